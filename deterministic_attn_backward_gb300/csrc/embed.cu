@@ -1275,8 +1275,9 @@ extern "C" dab_status_t dab_embed_bwd(const void* ids, dab_dtype_t ids_type, con
   if (!index_type(ids_type) || !float_type(dout_type) || !float_type(grad_type)) return DAB_ERR_INVALID_ARG;
   if (accumulate != 0 && accumulate != 1) return DAB_ERR_INVALID_ARG;
   if (!grad_layout(n, rows, width, &L)) return DAB_ERR_INVALID_ARG;
-  if (n > 0 && width > 0 && (!is_aligned(ids, ids_type == DAB_I64 ? 8 : 4) || !is_aligned(dout, 16)))
-    return DAB_ERR_INVALID_ARG;
+  // the tokens are read whatever the width, for those outside the table
+  if (n > 0 && !is_aligned(ids, ids_type == DAB_I64 ? 8 : 4)) return DAB_ERR_INVALID_ARG;
+  if (n > 0 && width > 0 && !is_aligned(dout, 16)) return DAB_ERR_INVALID_ARG;
   if (rows > 0 && width > 0 && !is_aligned(grad, 16)) return DAB_ERR_INVALID_ARG;
   if (!is_aligned(workspace, 16) || ws_bytes < L.total) return DAB_ERR_WORKSPACE;
   int sms = 0;

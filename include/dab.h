@@ -461,8 +461,9 @@ size_t dab_embed_bwd_workspace_size(int64_t n, int64_t rows, int width);
  * then the segments' sums in order; the result is rounded once to grad_type.
  * So every call gives the same bits.  Tokens equal to `padding` (a number
  * outside [0, rows) for none) get no gradient; tokens outside [0, rows) get
- * none either and DAB_ERR_DEVICE_BOUNDS from dab_check_status().  dout: n x
- * width, grad: rows x width, BF16 or F32 each, contiguous, 16-byte aligned.  */
+ * none either and DAB_ERR_DEVICE_BOUNDS from dab_check_status() (also with
+ * width 0: the tokens are always read).  dout: n x width, grad: rows x width,
+ * BF16 or F32 each, contiguous, 16-byte aligned.                            */
 dab_status_t dab_embed_bwd(const void* ids, dab_dtype_t ids_type,
                            const void* dout, dab_dtype_t dout_type,
                            void* grad, dab_dtype_t grad_type,
