@@ -39,6 +39,7 @@ cudaError_t launch_convert(const float* dqacc, int chunk_major, void* dq, int nt
 cudaError_t launch_block_tables(const uint8_t* tiles, int N, int causal, int descending,
                                 uint16_t* list, uint16_t* rank, int* nact, int* count,
                                 cudaStream_t stream);
+cudaError_t launch_limit_status(WsHeader* hdr, cudaStream_t stream);
 cudaError_t launch_limit_tables(const int* limit, int T, int N, int* lim, int* lmin, int* lmax, WsHeader* hdr,
                                 cudaStream_t stream);
 cudaError_t launch_limit_ranks(const int* lmax, int N, uint8_t* late, int2* units, uint16_t* rank, int* count,
@@ -370,17 +371,20 @@ static dab_status_t fwd_impl(const void* q, const void* k, const void* v, void* 
     // each other's softmax, but wait for each other too.  (4 heads of 4096 tokens:
     // 52 us against 68; 9: 61 against 73; 12: 79 against 74.)
     p.single = (long long)p.BH * p.N <= 2ll * sms ? 1 : 0;
-    if (p.N > dab::kLimSmallTiles) {  // otherwise the kernel reads them itself
+    cudaError_t e;
+    if (p.N > dab::kLimSmallTiles) {
       uint8_t* ws = static_cast<uint8_t*>(workspace);
       int* lim = reinterpret_cast<int*>(ws + T.lim);
       int* lmin = reinterpret_cast<int*>(ws + T.lmin);
       int* lmax = reinterpret_cast<int*>(ws + T.lmax);
-      const cudaError_t e = dab::launch_limit_tables(limit, tokens, p.N, lim, lmin, lmax, hdr, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "limit table launch");
+      e = dab::launch_limit_tables(limit, tokens, p.N, lim, lmin, lmax, hdr, stream);
       p.lim = lim;
       p.lmin = lmin;
       p.lmax = lmax;
+    } else {  // the kernel reads the limits itself
+      e = dab::launch_limit_status(hdr, stream);
     }
+    if (e != cudaSuccess) return cuda_fail(e, "limit table launch");
   } else if (hdr != nullptr && cudaMemsetAsync(hdr, 0, 16, stream) != cudaSuccess) {
     return DAB_ERR_CUDA;
   }
@@ -390,8 +394,8 @@ static dab_status_t fwd_impl(const void* q, const void* k, const void* v, void* 
   const void* kernel = d == 128 ? dab::fwd_kernel_ptr<128>(limits) : dab::fwd_kernel_ptr<64>(limits);
   const int smem = d == 128 ? dab::fwd_smem_bytes<128>(limits) : dab::fwd_smem_bytes<64>(limits);
   cudaError_t e;
-  if (p.lim != nullptr) {
-    // it may start while the tables are made (it waits for them)
+  if (limits) {
+    // it may start while the launch before ends (it waits for that one)
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;

@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (hdr == nullptr) hdr = &g_fwd_status;
   if ((sbase & 1023u) != 0u) {
+    if (kLim) grid_wait();  // the launch that clears the status
     if (threadIdx.x == 0) raise_error(hdr, kStatusBounds, kDetailAlign);
     return;
   }
@@ -217,12 +218,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
   }
   if (kLim) {
     if (lim_small) {
-      // CTA 0 clears the status for all: nothing else of this launch reports
-      // before a wait of seconds has run out
-      if (blockIdx.x == 0 && threadIdx.x == 0) {
-        hdr->status = 0u;
-        hdr->detail = 0u;
-      }
       for (int c = threadIdx.x; c < p.N * kTile; c += kFwdThreads)
         s_lim[c] = c < rows ? limit_len(__ldg(p.limit + c), c, rows) : 0;
       __syncthreads();
@@ -242,9 +237,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
         }
       }
       __syncthreads();
-    } else {
-      grid_wait();  // the tables' launch
     }
+    // The launch that made the tables or cleared the status word, which every
+    // bounded wait below may read.
+    grid_wait();
     for (int w = warp; w * 32 < nkv; w += kFwdThreads / 32) {
       const int c = w * 32 + lane;
       const int reach = c < nkv ? lmax[c] : 0;  // KV tile c is seen by the rows of its keys and on, below this one
