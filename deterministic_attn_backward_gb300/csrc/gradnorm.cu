@@ -344,12 +344,22 @@ __device__ __forceinline__ float total_norm(const Sum* sums, int n, Pair* sh) {
   return sqrtf(block_sum(v, sh).value()) * (big ? 0x1p90f : some ? 0x1p10f : 0x1p-80f);
 }
 
+// These kernels have no device-side error to report: the last launch of a call
+// leaves the workspace's status clear, for whoever reads it.
+__device__ __forceinline__ void clear_status(WsHeader* hdr) {
+  hdr->status = 0u;
+  hdr->detail = 0u;
+}
+
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Sum* __restrict__ sums, int n,
-                                                             float* __restrict__ norm) {
+                                                             float* __restrict__ norm, WsHeader* __restrict__ hdr) {
   __shared__ Pair sh[kThreads / 32];
   grid_wait();
   const float v = total_norm(sums, n, sh);
-  if (threadIdx.x == 0) *norm = v;
+  if (threadIdx.x == 0) {
+    *norm = v;
+    clear_status(hdr);
+  }
 }
 
 // Scales `cells` (at most kBatch) cells of a tensor.
@@ -384,12 +394,16 @@ __device__ __forceinline__ void scale_cells(const T* src, T* dst, unsigned long 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_constant__ Table<N> t,
                                                                  const Sum* __restrict__ sums, int n_sums,
-                                                                 const float* given, float* norm, float max_norm) {
+                                                                 const float* given, float* norm, float max_norm,
+                                                                 WsHeader* __restrict__ hdr) {
   __shared__ Pair sh[kThreads / 32];
   const uint32_t batches = batches_of(t);
   grid_wait();
   const float v = sums != nullptr ? total_norm(sums, n_sums, sh) : *given;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *norm = v;
+    clear_status(hdr);
+  }
   const float q = max_norm / (v + 1e-6f);
   const float f = q >= 1.f ? 1.f : q;  // a norm that is no number makes the gradients none
   if (f == 1.f && t.in_place) return;  // x * 1 is x (walking the batches took 10 us for 512 MB)
@@ -516,7 +530,7 @@ cudaError_t norm_pass(const dab_grad_t* grads, int count, Sum* sums, int* n_sums
 
 template <int N>
 cudaError_t clip_pass(const dab_grad_t* grads, int count, float max_norm, const float* given, float* norm,
-                      Sum* sums, cudaStream_t stream) {
+                      Sum* sums, WsHeader* hdr, cudaStream_t stream) {
   int n_sums = 0;
   cudaError_t e = cudaSuccess;
   if (given == nullptr && (e = norm_pass<N>(grads, count, sums, &n_sums, stream)) != cudaSuccess) return e;
@@ -527,7 +541,7 @@ cudaError_t clip_pass(const dab_grad_t* grads, int count, float max_norm, const 
     fill(&t, grads, k, std::min(count, k + N));
     if (t.count == 0) continue;
     e = launch(grad_scale_kernel<N>, ctas_of(t), kThreads, stream, first && given == nullptr, t, add, n_sums, given,
-               norm, max_norm);
+               norm, max_norm, hdr);
     first = false;
   }
   return e;
@@ -550,10 +564,12 @@ extern "C" dab_status_t dab_grad_norm(const dab_grad_t* grads, int count, float*
   if (!is_aligned(workspace, 16) || ws_bytes < norm_workspace(count)) return DAB_ERR_WORKSPACE;
   if (!device_ready(nullptr)) return DAB_ERR_UNSUPPORTED;
   Sum* sums = reinterpret_cast<Sum*>(static_cast<uint8_t*>(workspace) + kOffSums);
+  WsHeader* hdr = static_cast<WsHeader*>(workspace);
   int n_sums = 0;
   cudaError_t e = count <= kSmall ? norm_pass<kSmall>(grads, count, sums, &n_sums, stream)
                                   : norm_pass<kLarge>(grads, count, sums, &n_sums, stream);
-  if (e == cudaSuccess) e = launch(grad_norm_kernel, 1, kThreads, stream, n_sums > 0, (const Sum*)sums, n_sums, norm);
+  if (e == cudaSuccess)
+    e = launch(grad_norm_kernel, 1, kThreads, stream, n_sums > 0, (const Sum*)sums, n_sums, norm, hdr);
   return e == cudaSuccess ? DAB_OK : record_cuda_error(e, "gradient norm launch");
 }
 
@@ -568,14 +584,19 @@ extern "C" dab_status_t dab_grad_clip(const dab_grad_t* grads, int count, float 
   if (!is_aligned(workspace, 16) || ws_bytes < norm_workspace(count)) return DAB_ERR_WORKSPACE;
   if (!device_ready(nullptr)) return DAB_ERR_UNSUPPORTED;
   Sum* sums = reinterpret_cast<Sum*>(static_cast<uint8_t*>(workspace) + kOffSums);
+  WsHeader* hdr = static_cast<WsHeader*>(workspace);
   cudaError_t e;
   if (cells == 0) {  // nothing to scale: only the norm is written
-    if (given == nullptr) e = launch(grad_norm_kernel, 1, kThreads, stream, false, (const Sum*)sums, 0, norm);
-    else e = given == norm ? cudaSuccess
-                           : cudaMemcpyAsync(norm, given, sizeof(float), cudaMemcpyDeviceToDevice, stream);
+    if (given == nullptr) {
+      e = launch(grad_norm_kernel, 1, kThreads, stream, false, (const Sum*)sums, 0, norm, hdr);
+    } else {
+      e = cudaMemsetAsync(hdr, 0, 8, stream);
+      if (e == cudaSuccess && given != norm)
+        e = cudaMemcpyAsync(norm, given, sizeof(float), cudaMemcpyDeviceToDevice, stream);
+    }
   } else {
-    e = count <= kSmall ? clip_pass<kSmall>(grads, count, max_norm, given, norm, sums, stream)
-                        : clip_pass<kLarge>(grads, count, max_norm, given, norm, sums, stream);
+    e = count <= kSmall ? clip_pass<kSmall>(grads, count, max_norm, given, norm, sums, hdr, stream)
+                        : clip_pass<kLarge>(grads, count, max_norm, given, norm, sums, hdr, stream);
   }
   return e == cudaSuccess ? DAB_OK : record_cuda_error(e, "gradient clip launch");
 }

@@ -251,8 +251,8 @@ dab_status_t dab_attn_bwd_limit(const void* q, const void* k, const void* v,
                                 void* workspace, size_t ws_bytes,
                                 cudaStream_t stream);
 
-/* Synchronises `stream`, then reads the status word that the backward kernels
- * of the last call on this workspace wrote.  Returns DAB_OK, DAB_ERR_TIMEOUT
+/* Synchronises `stream`, then reads the status word that the kernels of the
+ * last call on this workspace wrote.  Returns DAB_OK, DAB_ERR_TIMEOUT
  * or DAB_ERR_DEVICE_BOUNDS (or DAB_ERR_CUDA if the synchronisation failed).  */
 dab_status_t dab_check_status(const void* workspace, cudaStream_t stream);
 
