@@ -633,7 +633,9 @@ class GradList:
     """A list of gradient tensors as the library takes it, with a workspace of
     its own: made once for gradients that stay where they are and passed to
     grad_norm() and clip_grads() in every step.  `out`: where the clipped
-    gradients go (in place if not given).  One list serves one stream at a time."""
+    gradients go (in place if not given).  One list serves one stream at a time,
+    which need not be the one it was made on, and outlives the graphs that
+    captured a call with it."""
 
     def __init__(self, grads, out=None):
         lib = load_library()
@@ -654,9 +656,16 @@ class GradList:
         if size == 0:
             raise DabError(1, "dab_grad_workspace_size")
         self.device = torch.device("cuda", self.index)
+        self.stream = torch._C._cuda_getCurrentRawStream(self.index)    # that the workspace belongs to
         self.workspace = torch.empty(size, dtype=_U8, device=self.device)
         self.args = (self.array, len(self.grads))
         self.ws = (self.workspace.data_ptr(), size)
+
+    def _used(self):
+        """Before a call: keeps the workspace's memory from being handed out, once the
+        list is dropped, before the current stream is done with it."""
+        if torch._C._cuda_getCurrentRawStream(self.index) != self.stream:
+            self.workspace.record_stream(torch.cuda.current_stream(self.device))
 
 
 def grad_norm(grads, out=None) -> torch.Tensor:
@@ -666,6 +675,7 @@ def grad_norm(grads, out=None) -> torch.Tensor:
     if not isinstance(grads, GradList):
         grads = GradList(grads)
     norm = torch.empty((), dtype=_F32, device=grads.device) if out is None else _scalar(out, grads.index, "out")
+    grads._used()
     _run(grads.index, lib.dab_grad_norm, *grads.args, norm.data_ptr(), *grads.ws)
     return norm
 
@@ -680,6 +690,7 @@ def clip_grads(grads, max_norm, norm=None) -> torch.Tensor:
         grads = GradList(grads)
     given = None if norm is None else _scalar(norm, grads.index, "norm").data_ptr()
     total = torch.empty((), dtype=_F32, device=grads.device)
+    grads._used()
     _run(grads.index, lib.dab_grad_clip, *grads.args, max_norm, given, total.data_ptr(), *grads.ws)
     return total
 
