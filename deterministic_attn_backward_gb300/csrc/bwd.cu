@@ -140,7 +140,7 @@ static __device__ __noinline__ bool sem_wait(const uint32_t* sem, uint32_t targe
 template <bool kLim>
 __device__ __forceinline__ int k_unit(const BwdParams& p, int U, int& bh, int& u, bool& ascending) {
   if (kLim) {
-    const int2 e = __ldg(p.lim_units + U / p.BH);
+    const int2 e = p.lim_units[U / p.BH];
     bh = U % p.BH;
     u = e.x & ~kLimAscending;
     ascending = e.x != u || p.sched != kSchedDescending;
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant_
         const float* dd = s_dd + stage * 128 + 64 * h;
         // a tile with hidden pairs: the causal diagonal, or (key limits) also
         // one where some key's limit lies before the end of the Q tile
-        const bool diag = kLim ? (st.kv == st.q || __ldg(p.lmin + st.kv) < min((st.q + 1) * kTile, p.T))
+        const bool diag = kLim ? (st.kv == st.q || p.lmin[st.kv] < min((st.q + 1) * kTile, p.T))
                                : (p.mask == kMaskCausal) && (st.kv == st.q);
         // key limits: Q columns lo <= qc < lo + span of the tile see this key
         int lo = 0;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant_
         if (kLim && diag) {
           const int key = st.kv * kTile + r;
           lo = key - st.q * kTile;
-          span = (uint32_t)__ldg(p.lim + key);
+          span = (uint32_t)p.lim[key];
         }
         // a key past the end of a partial last tile: its whole P row is 0
         // (applied to the packed words below; `key_out` only on such a tile)
