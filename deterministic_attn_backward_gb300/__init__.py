@@ -306,6 +306,22 @@ def _run(index, fn, *args):
         raise DabError(code, fn.__name__)
 
 
+def _copied(t, dev):
+    """t on the device, contiguous, with the values it has now: the copy from pinned
+    memory is asynchronous, so it is taken from a snapshot that the caller cannot
+    refill meanwhile (from other host memory it is staged before the call returns).
+    A graph under capture copies from the caller's pinned memory in every replay."""
+    if t.device.type == "cpu" and t.is_pinned() and not torch.cuda.is_current_stream_capturing():
+        t = torch.empty(t.shape, dtype=t.dtype, pin_memory=True).copy_(t)
+    return t.to(dev, non_blocking=True).contiguous()
+
+
+def _own_bf16(t, index, dev):
+    if t.dtype is not _BF16:
+        raise TypeError("expected bfloat16 tensors")
+    return t if _ready(t, _BF16, index) else _copied(t, dev)
+
+
 def _limit(limit, mask, S, dev):
     """Key limits as a contiguous int32 [S] CUDA tensor."""
     t = limit if isinstance(limit, torch.Tensor) else torch.as_tensor(limit)
@@ -317,7 +333,7 @@ def _limit(limit, mask, S, dev):
         if t.dtype.is_floating_point or t.dtype.is_complex or t.dtype == torch.bool:
             raise TypeError("limit must hold whole numbers")
         t = t.clamp(0, S).to(_I32)
-    return t if t.device == dev and t.is_contiguous() else t.to(dev, non_blocking=True).contiguous()
+    return t if t.device == dev and t.is_contiguous() else _copied(t, dev)
 
 
 def attn_fwd(q, k, v, mask="full", scale=None, workspace=None, out=None, lse=None, tiles=None, limit=None,
@@ -380,7 +396,7 @@ def _attn_fwd_limit(q, k, v, mask, scale, workspace, out, lse, tiles, limit, tok
     index = q.get_device() if q.is_cuda else torch.cuda.current_device()
     dev = q.device if q.is_cuda else torch.device("cuda", index)
     if not (_ready(q, _BF16, index) and _ready(k, _BF16, index) and _ready(v, _BF16, index)):
-        q, k, v = (_dev_bf16(t, dev) for t in (q, k, v))
+        q, k, v = (_own_bf16(t, index, dev) for t in (q, k, v))
     lim = _limit(limit, mask, S, dev)
     tokens = _tokens(tokens, S)
     new = torch.empty if tokens == S else torch.zeros
@@ -517,11 +533,11 @@ def _attn_bwd_limit(q, k, v, o, lse, dout, mask, sched, scale, workspace, out, o
     index, dev = q.get_device(), q.device
     if not (_ready(q, _BF16, index) and _ready(k, _BF16, index) and _ready(v, _BF16, index)
             and _ready(o, _BF16, index) and _ready(dout, _BF16, index)):
-        q, k, v, o, dout = (_dev_bf16(t, dev) for t in (q, k, v, o, dout))
+        q, k, v, o, dout = (_own_bf16(t, index, dev) for t in (q, k, v, o, dout))
     if not _ready(lse, _F32, index):
         if lse.dtype is not _F32:
             raise TypeError("lse must be float32")
-        lse = lse.to(dev, non_blocking=True).contiguous()
+        lse = _copied(lse, dev)
     lim = _limit(limit, mask, S, dev)
     if workspace is None:
         workspace = new_workspace(B, H, S, d, mask, sched, dev, limit=True)
@@ -559,7 +575,7 @@ def _ids(ids, index, dev):
     if code is None:
         raise TypeError("ids must be int32 or int64")
     if ids.get_device() != index or not ids.is_contiguous():
-        ids = ids.to(dev, non_blocking=True).contiguous()
+        ids = _copied(ids, dev)
     return ids, code
 
 
