@@ -281,6 +281,7 @@ def prefix_limits(lengths, parents=None) -> torch.Tensor:
 # The checks of the calls below cost as much as the calls when they go through
 # tensors' slower accessors: dtypes are compared as objects, devices by index.
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_WHOLE = (torch.int64, torch.int16, torch.int8, torch.uint8)
 
 
 def _ready(t, dtype, index) -> bool:
@@ -330,9 +331,9 @@ def _limit(limit, mask, S, dev):
     if t.shape != (S,):
         raise ValueError("limit must be [S]")
     if t.dtype is not _I32:
-        if t.dtype.is_floating_point or t.dtype.is_complex or t.dtype == torch.bool:
+        if t.dtype not in _WHOLE:
             raise TypeError("limit must hold whole numbers")
-        t = t.clamp(0, S).to(_I32)
+        t = t.clamp(0, S).to(_I32) if t.dtype is torch.int64 else t.to(_I32)    # narrower ones fit as they are
     return t if t.device == dev and t.is_contiguous() else _copied(t, dev)
 
 
@@ -340,7 +341,8 @@ def attn_fwd(q, k, v, mask="full", scale=None, workspace=None, out=None, lse=Non
              tokens=None):
     """O (bf16 [B,H,S,d]) and LSE (f32 [B,H,S]) on q's CUDA device.
     `tiles`: optional block mask [S/128, S/128] (dab_attn_fwd_block).
-    `limit`: key limits [S] of packed sequences and shared prefixes, with
+    `limit`: key limits [S] of packed sequences and shared prefixes (int32, or
+    other signed whole numbers or uint8, which are converted), with
     mask="causal": key c is visible to the queries c <= q < limit[c]
     (dab_attn_fwd_limit; see prefix_limits).  `tokens`: with limit, how many rows
     of a head are in use; those behind them are not read, and stay as they are in
