@@ -41,11 +41,11 @@ DET_SCHEDS = ("serial", "descending_q", "shift")
 # heads, so the B=2 launch moves twice as much.  Reported only while the
 # source is unchanged.
 TRAFFIC_CAPTURES = {
-    "a1187a10e664449de754d08b0cce1bf6b0e2a036": {
-        "causal/serial": 461.5 + 401.4, "causal/descending_q": 393.0 + 350.6,
-        "causal/shift": 446.8 + 448.6, "causal/atomic": 202.8 + 88.3,
-        "full/serial": 399.1 + 363.4, "full/descending_q": 399.2 + 363.6,
-        "full/shift": 432.6 + 441.5, "full/atomic": 202.6 + 87.8,
+    "1ec4b00ecf6098d88485a44449f5376fc73499e8": {
+        "causal/serial": 445.7 + 392.8, "causal/descending_q": 392.7 + 350.5,
+        "causal/shift": 448.1 + 452.5, "causal/atomic": 202.7 + 88.1,
+        "full/serial": 399.0 + 364.5, "full/descending_q": 400.6 + 367.5,
+        "full/shift": 439.1 + 443.2, "full/atomic": 202.6 + 88.1,
     },
 }
 MASKS = ("causal", "full")
