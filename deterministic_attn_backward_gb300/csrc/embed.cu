@@ -51,16 +51,19 @@ constexpr int kSegment = 32;                    // tokens of a segment, up to kS
 constexpr int kSortRun = 8192;                  // runs up to this are sorted in shared memory
 
 // Up to kFewTokens tokens, and as long as a search of all of them for every token
-// and piece of a row takes at most kFewSteps, one launch does it all: quicker than
-// six launches up to there (1000 tokens of width 512: 9.5 us against 14.2, of 2048
-// 12.5 against 16.0, of 4096 18.4 against 16.2; 2048 of 64 13.2 against 14.3, of 512
-// 16.4 against 15.4, of 1024 18.1 against 15.1).
+// and piece of a row takes at most kFewSteps, one launch does it all.  One launch
+// against several, bf16 rows added to 1000 of f32, frequencies as 1 / rank: 1024
+// tokens of width 2048 12.1 us against 15.1, at the bound 2048 of 512 14.2 against
+// 15.3 (f32 rows 16.9 against 16.2); beyond it 2048 of 1024 17.0 against 15.9, but
+// 1500 of 1024 12.5 against 15.3 and 1024 of 4096 16.3 against 17.7.
 constexpr int kFewTokens = 2048;
 constexpr long long kFewSteps = 1ll << 23;
 // Up to this many tokens, long runs are gathered by walking all tokens, a CTA for
-// each run; beyond, they are scattered and sorted by a launch of their own.  65536
-// tokens of width 64, frequencies as 1 / rank: 40 us against 46 (1000 rows), 51
-// against 55 (131072); 1638 rows named evenly, more long runs than CTAs: 73 against 41.
+// each run; beyond, they are scattered and sorted by a launch of their own.  Walking
+// against sorting, 65536 tokens of width 64, frequencies as 1 / rank: 40 us against
+// 46 (1000 rows), 51 against 55 (131072).  How many long runs there are is known on
+// the device only, so the rule cannot look at it: 1638 rows named evenly, more long
+// runs than CTAs, take 73 us for 41.
 constexpr long long kWalkTokens = 65536;
 
 // Cursors, in the header's padding: short runs' places and short runs share one
@@ -1153,10 +1156,12 @@ cudaError_t launch_embed_fwd(const void* ids, const void* table, void* out, long
 
 // Whether rows of so many bytes are summed by the stream.  It starts 6 us later
 // than a warp per run does, and its copies, which an SM issues one after the
-// other, take some 45 ns each.  The gradient of bf16 rows up to the joining, in
-// us: 2500 of 1 KB 22 against 20, 16384 of 512 bytes 26 against 20, 65536 of them
-// 52 against 46; 65536 of 1 KB 54 either way, 8192 of 4 KB 44 against 47, 65536 of
-// them into 131072 rows 161 against 193.
+// other, take some 45 ns each.  Whole gradients, the stream against a warp per
+// run, bf16 rows added to f32 ones, frequencies as 1 / rank: at 32 MB 8192 of 4 KB
+// 42.5 us against 39.2 (dense 67.6 against 70.2) and 32768 of 1 KB 51.1 against
+// 43.8; beyond, 16384 of 4 KB into bf16 51.7 against 53.7 (dense 53.7 against 60.8),
+// 65536 of them into 131072 rows 160 against 175, where rows are shorter 32768 of 2
+// KB 61.9 against 59.1 and 65536 of 1 KB 74.4 against 67.3.
 bool streams(long long row_bytes, long long n) {
   return row_bytes % 16 == 0 && row_bytes >= 1024 && row_bytes * n > (1 << 25);
 }

@@ -22,6 +22,10 @@
 // 2^-63: a CTA whose sum came out infinite or tiny adds once more with its
 // elements scaled by a power of two, so the norm is right over the whole range
 // of the types.
+//
+// Tensors that are not aligned to 16 bytes (views into a flat buffer) are read and
+// written element by element: 118 MB in 32 tensors take 56 us aligned, 71 in f32 at
+// 4 bytes off and 176 to 190 in bf16 at 2 to 8 bytes off; the norm alone 21, 25 and 40.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -420,11 +420,11 @@ dab_status_t dab_attn_bwd_host(const void* q, const void* k, const void* v,
                                cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
-/* The rest of a reproducible training step: the embedding and the gradient
- * norm, the other two places where a step usually adds floats in whatever
- * order the GPU happens to run.  The paper's subject is the attention
- * backward; these keep its promise (the same bits from run to run) for the
- * step around it.  All sums are f32 or wider, in an order fixed by the inputs
+/* The rest of a reproducible training step: the embedding, whose gradient is
+ * usually added by float atomics in whatever order the GPU happens to run, and
+ * the gradient norm, whose order usually follows the launch's grid.  The
+ * paper's subject is the attention backward; these keep its promise (the same
+ * bits from run to run) for the step around it.  All sums are f32 or wider, in an order fixed by the inputs
  * alone.                                                                     */
 typedef enum {
     DAB_BF16 = 0,

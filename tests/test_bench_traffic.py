@@ -6,7 +6,7 @@ import pytest
 import bench
 
 
-@pytest.mark.parametrize("causal,full", itertools.product(bench.ALL_SCHEDS, repeat=2))
+@pytest.mark.parametrize("causal,full", list(itertools.product(bench.ALL_SCHEDS, repeat=2)))
 def test_every_pair_of_schedules_has_its_traffic(causal, full):
     """Null means that csrc/bwd.cu changed after the captures: capture again (the
     command is in profiles/bwd_main_per_schedule_b1h16s8192d128_b4h16s2048d64.md)."""
