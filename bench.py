@@ -41,11 +41,11 @@ DET_SCHEDS = ("serial", "descending_q", "shift")
 # heads, so the B=2 launch moves twice as much.  Reported only while the
 # source is unchanged.
 TRAFFIC_CAPTURES = {
-    "1ec4b00ecf6098d88485a44449f5376fc73499e8": {
-        "causal/serial": 445.7 + 392.8, "causal/descending_q": 392.7 + 350.5,
-        "causal/shift": 448.1 + 452.5, "causal/atomic": 202.7 + 88.1,
-        "full/serial": 399.0 + 364.5, "full/descending_q": 400.6 + 367.5,
-        "full/shift": 439.1 + 443.2, "full/atomic": 202.6 + 88.1,
+    "9e74789408e67c374956a5c8030e9fd38699f15e": {
+        "causal/serial": 449.8 + 384.9, "causal/descending_q": 394.2 + 352.2,
+        "causal/shift": 446.5 + 450.2, "causal/atomic": 202.7 + 88.2,
+        "full/serial": 398.7 + 362.6, "full/descending_q": 400.8 + 367.5,
+        "full/shift": 434.7 + 441.3, "full/atomic": 203.0 + 88.3,
     },
 }
 MASKS = ("causal", "full")

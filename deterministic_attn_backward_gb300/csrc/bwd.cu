@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant_
 
   // Operand tiles need 1024-byte-aligned swizzle atoms.
   if ((sbase & 1023u) != 0u) {
+    if (kLim) grid_wait();  // the launch that clears the status
     if (threadIdx.x == 0) raise_error(p.hdr, kStatusBounds, kDetailAlign);
     return;
   }
