@@ -46,7 +46,7 @@ def test_a_pinned_buffer_may_be_refilled_after_the_call(name):
     call(*[pinned(t) for t in host])                    # the pinned memory that the calls need is there
     held = [pinned(t) for t in host]
     torch.cuda.synchronize()
-    torch.cuda._sleep(40_000_000)                       # some 20 ms
+    torch.cuda._sleep(100_000_000)                      # some 50 ms
     done = torch.cuda.Event()
     got = call(*held)
     done.record()
